@@ -325,7 +325,7 @@ def _distill_plain(state):
         tmax = t.amax(1, keepdim=True)
         lse_t = tmax + torch.log(torch.exp(t - tmax).sum(1, keepdim=True))
     logp = t - lse_t
-    p = torch.exp(logp)
+    p = torch.where(there, torch.exp(logp), 0.0)  # a row without entries: all 0
     logq = (z.gather(1, at) - zmax) / tau - torch.log(sz)
     kl = torch.where(there, p * (logp - logq), 0.0).sum(1)
     loss = soft * tau * tau * kl
@@ -432,7 +432,8 @@ def _distill_exact(state, zero):
         t[idx < 0] = float("-inf")
         lse = (state["lse"][s].double()[:, None] if state["lse"] is not None
                else torch.logsumexp(t, 1, keepdim=True))
-        probs = torch.exp(t - lse)
+        # a row without entries has lse = -inf and no probability anywhere
+        probs = torch.where(idx >= 0, torch.exp(t - lse), 0.0)
         dense = torch.zeros_like(z).scatter_add_(1, idx.clamp(min=0), probs)
         picked = torch.gather(lsm, 1, idx.clamp(min=0))
         terms = torch.where(probs > 0, probs * (t - lse - picked), 0.0)
