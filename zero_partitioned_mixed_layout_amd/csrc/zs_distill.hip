@@ -543,8 +543,12 @@ __global__ __launch_bounds__(NT, NV <= 8 ? 8 : 4) void zs_distill_kernel(Distill
     if (hi == V && tid < rest) {
         out[(uint64_t)nv * E + tid] = g.at(last[0]);
     }
-    if (g.check) { // rare: look through what this thread wrote
-        for (uint32_t i = v0 + tid; i < v1 && !bad; i += NT)
+    if (g.check) { // rare: look through what this thread wrote, and nothing else:
+                   // no barrier lies between.  From registers it wrote the vectors
+                   // that are tid mod NT.
+        static_assert((NT & (NT - 1)) == 0, "tid - v0 wraps");
+        const uint32_t first = v0 + (NV > 0 ? (tid - v0) % NT : tid);
+        for (uint32_t i = first; i < v1 && !bad; i += NT)
             for (uint32_t e = 0; e < E && !bad; e++)
                 bad = nonfinite(out[(uint64_t)i * E + e]) &&
                       counts(a, sh, label, (uint64_t)i * E + e);
