@@ -631,6 +631,13 @@ def _launch(fn: str, index: int, stream, *args) -> None:
         raise ZeroError(fn, rc)
 
 
+def _torch_stream(handle: int, device):
+    """torch's stream of a handle.  Handle 0 is the default stream; torch takes
+    an external 0 for none given and makes a stream of its own pool."""
+    return torch.cuda.ExternalStream(handle, device) if handle else \
+        torch.cuda.default_stream(device)
+
+
 def _rows(t: torch.Tensor, what: str, types: dict, index: Optional[int] = None):
     """(pointer, types' entry, rows, cols, pitch) of a device tensor of one or
     two dimensions whose rows are contiguous; one dimension is a single row."""
@@ -804,7 +811,7 @@ def zero_mxfp4_linear_grad_input(dy: torch.Tensor, w: MXFP4, out: torch.Tensor,
     if stream is None:
         ws = torch.empty(need.value, dtype=torch.uint8, device=w.device)
     else:  # the allocator orders the memory's next use after this stream's work
-        with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), w.device)):
+        with torch.cuda.stream(_torch_stream(_stream_handle(stream), w.device)):
             ws = torch.empty(need.value, dtype=torch.uint8, device=w.device)
     _launch("zero_mxfp4_linear_grad_input", i, stream, dp, dt, m, ldd, w._ref, p, ty, ld,
             ws.data_ptr(), need.value)
