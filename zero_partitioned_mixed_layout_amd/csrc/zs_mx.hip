@@ -2069,7 +2069,9 @@ extern "C" int zero_mxfp4_linear_grad_input(const void *dy, int dy_type, uint64_
         return ZERO_EINVAL;
     if ((uintptr_t)workspace + workspace_bytes < (uintptr_t)workspace)
         return ZERO_EOVERFLOW;
-    r[4] = {(uintptr_t)workspace, (uintptr_t)workspace + workspace_bytes, true};
+    r[4] = {0, 0, true}; // no bytes overlap nothing
+    if (workspace_bytes)
+        r[4] = {(uintptr_t)workspace, (uintptr_t)workspace + workspace_bytes, true};
     if ((rc = matrix_range(dy, dy_type, m, w->rows, ld_dy, false, &r[2])) != ZERO_OK ||
         (rc = matrix_range(dx, dx_type, m, w->cols, ld_dx, true, &r[3])) != ZERO_OK ||
         (rc = check_product(r, 5, m, ld_dy, w)) != ZERO_OK)
