@@ -8,10 +8,10 @@ import sys
 
 import pytest
 
-from test_mx_distill_host import B, EHIP, EINVAL, F16, F32, ROOT, mx
+from test_mx_distill_host import B, EHIP, EINVAL, EOVERFLOW, F16, F32, ROOT, mx
 
 
-@pytest.mark.parametrize("body", ["empty_workspace"])
+@pytest.mark.parametrize("body", ["empty_workspace", "many_rows"])
 def test_limits(body):
     env = dict(os.environ, HIP_VISIBLE_DEVICES="", CUDA_VISIBLE_DEVICES="",
                ROCR_VISIBLE_DEVICES="")
@@ -36,3 +36,23 @@ def empty_workspace(zs):
     for at in (x + 8, y + 8, B + 64, B + (1 << 36) + 4, 9 * B):
         assert grad(at, 0) == EHIP, hex(at)
     assert grad(x + 8, 4) == EINVAL and grad(x + 2, 0) == EINVAL and grad(9 * B, 64) == EHIP
+
+
+def many_rows(zs):
+    """Weights of up to 2^30 rows, short ones among them, for any number of
+    rows of the left operand that takes the kernels for few."""
+    L = zs.lib()
+    for n in ((1 << 27) - 16, (1 << 27) + 1, 1 << 28, 1 << 30):
+        for k in (1, 32, 224, 256):
+            nb = -(-k // 32)
+            w = mx(zs, n, k, scales=B + (1 << 39))
+            for m in (1, 17, 32):
+                a = mx(zs, m, k, base=3 * B)
+                assert n * 16 * nb < 1 << 39 and m * n * 4 < B
+                assert L.zero_mxfp4_matmul(ctypes.byref(a), ctypes.byref(w), 7 * B, F32, n,
+                                           None) == EHIP, (m, n, k)
+                assert L.zero_mxfp4_linear(5 * B, F16, m, k, ctypes.byref(w), 7 * B, F32, n,
+                                           None) == EHIP, (m, n, k)
+    w = mx(zs, (1 << 30) + 1, 32, scales=B + (1 << 39))
+    assert L.zero_mxfp4_linear(5 * B, F16, 1, 32, ctypes.byref(w), 7 * B, F32, 1 << 31,
+                               None) == EOVERFLOW

@@ -354,6 +354,13 @@ __device__ __forceinline__ void skinny_join(f32x4 (&acc)[MT], f32x4 *lds, uint64
     }
 }
 
+// The first of this workgroup's 16 columns: a launch has at most kSkinnyGridX
+// workgroups along x (HIP counts a dimension's threads in 32 bits), the rest along y.
+constexpr uint64_t kSkinnyGridX = 1ull << 22;
+__device__ __forceinline__ uint64_t skinny_columns() {
+    return ((uint64_t)blockIdx.y * kSkinnyGridX + blockIdx.x) * 16u;
+}
+
 // This wave's share of the steps.
 __device__ __forceinline__ uint32_t skinny_first(uint32_t steps, uint32_t wave) {
     return steps * wave / kSkinnyWaves;
@@ -368,7 +375,9 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void zs_mx_matmul_skinny_kernel(
     __shared__ f32x4 lds[kSkinnyWaves * MT * 64];
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint64_t n0 = (uint64_t)blockIdx.x * 16u, n = n0 + r < N ? n0 + r : N - 1;
+    const uint64_t n0 = skinny_columns(), n = n0 + r < N ? n0 + r : N - 1;
+    if (n0 >= N)
+        return;
     const uint8_t *wc = w.codes + n * w.ld_codes, *ws = w.scales + n * w.ld_scales;
     f32x4 acc[MT];
     const uint8_t *ac[MT], *as[MT];
@@ -463,7 +472,9 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void zs_mx_linear_skinny_kernel(
     __shared__ f32x4 lds[kSkinnyWaves * MT * 64];
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint64_t n0 = (uint64_t)blockIdx.x * 16u, n = n0 + r < N ? n0 + r : N - 1;
+    const uint64_t n0 = skinny_columns(), n = n0 + r < N ? n0 + r : N - 1;
+    if (n0 >= N)
+        return;
     const uint8_t *wc = w.codes + n * w.ld_codes, *ws = w.scales + n * w.ld_scales;
     f32x4 acc[MT];
     const typename Fmt::T *xr[MT];
@@ -1794,6 +1805,13 @@ static int check_product(zs::Range *r, size_t n, uint64_t m, uint64_t pitch,
         }                                                                                          \
     } while (0)
 
+static dim3 skinny_grid(uint64_t N) {
+    const uint64_t groups = (N + 15) / 16;
+    return groups <= kSkinnyGridX
+               ? dim3((uint32_t)groups)
+               : dim3((uint32_t)kSkinnyGridX, (uint32_t)((groups + kSkinnyGridX - 1) / kSkinnyGridX));
+}
+
 // Tiles of a tiled product: 256 x 256 if they take more than half of the
 // chip's 256 CUs (one of them a CU), else 128 x 128 if there are `least` of
 // those (two a CU), else 64 x 64.  Measured at K = 4096, N = 4096, bfloat16
@@ -1896,13 +1914,10 @@ extern "C" int zero_mxfp4_matmul(const zero_mxfp4 *a, const zero_mxfp4 *w, void 
     if (M <= 32 && in_registers(nb, 4))
         ZS_CALL(4, 2, 4);
 #undef ZS_CALL
-    const uint64_t grid = (N + 15) / 16;
-    if (grid > zs::kMaxWorkgroups512)
-        return ZERO_EOVERFLOW;
+    const dim3 grid = skinny_grid(N);
 #define ZS_CALL(MT)                                                                                \
-    hipLaunchKernelGGL((zs_mx_matmul_skinny_kernel<MT>), dim3((uint32_t)grid),                     \
-                       dim3(kSkinnyWaves * 64), 0, st, mx_args(a), mx_args(w), M, N, (uint32_t)nb, \
-                       y, y_type, ld_y)
+    hipLaunchKernelGGL((zs_mx_matmul_skinny_kernel<MT>), grid, dim3(kSkinnyWaves * 64), 0, st,     \
+                       mx_args(a), mx_args(w), M, N, (uint32_t)nb, y, y_type, ld_y)
     ZS_BY_MT(M, ZS_CALL);
 #undef ZS_CALL
     return launch_status();
@@ -1958,13 +1973,11 @@ static int linear(const void *x, uint64_t m, uint64_t ld_x, const zero_mxfp4 *w,
     if (m <= 32 && in_registers(nb, 4))
         ZS_CALL(4, 2, 2);
 #undef ZS_CALL
-    const uint64_t grid = (N + 15) / 16;
-    if (grid > zs::kMaxWorkgroups512)
-        return ZERO_EOVERFLOW;
+    const dim3 grid = skinny_grid(N);
 #define ZS_CALL(MT)                                                                                \
-    hipLaunchKernelGGL((zs_mx_linear_skinny_kernel<Fmt, MT>), dim3((uint32_t)grid),                \
-                       dim3(kSkinnyWaves * 64), 0, st, (const typename Fmt::T *)x, ld_x,           \
-                       mx_args(w), m, N, (uint32_t)K, (uint32_t)nb, y, y_type, ld_y)
+    hipLaunchKernelGGL((zs_mx_linear_skinny_kernel<Fmt, MT>), grid, dim3(kSkinnyWaves * 64), 0,    \
+                       st, (const typename Fmt::T *)x, ld_x, mx_args(w), m, N, (uint32_t)K,        \
+                       (uint32_t)nb, y, y_type, ld_y)
     ZS_BY_MT(m, ZS_CALL);
 #undef ZS_CALL
     return launch_status();
