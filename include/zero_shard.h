@@ -696,6 +696,10 @@ int zero_gather_shards_mxfp4(const void *const *codes, const void *const *scales
  * type (ZERO_F16, ZERO_BF16 or ZERO_F32).  The order of a sum depends on the
  * sizes alone, so equal calls give equal bits.  Infinities and NaN follow
  * IEEE: a NaN block of w (scale byte 255) makes every output it enters NaN.
+ * A value of 2^128 or more, which only the scale bytes 253 and 254 reach and
+ * zero_mxfp4_quantize never writes, is past fp32: with a 16-bit operand it is
+ * an infinity and makes every output it enters infinite or NaN.
+ * zero_mxfp4_matmul takes it as it is.
  * Outputs are written only inside their m rows and their columns.  Sizes
  * up to 2^30 each, row pitches of x, dy (elements) and of 4-bit operands
  * (bytes) up to 2^23.  K = 0 (for the gradient N = 0) writes zeros; no output

@@ -43,3 +43,60 @@ def test_weights_of_more_rows_than_a_launch_dimension(zs, k):
         del y, whole, tail
     del w
     torch.cuda.empty_cache()
+
+
+def top_scales(zs, n, k, seed):
+    """A weight with blocks of scale bytes 253 and 254 in the first, a middle
+    and the last block of some rows: finite ones (codes up to 1.5 times 2^127)
+    in rows 1 and n // 2, ones past 2^128 in rows 2 and n - 1.  All codes are
+    positive.  (handle, fp64 values)."""
+    import torch
+    rng = np.random.default_rng(seed)
+    nb = -(-k // 32)
+    code = rng.integers(1, 8, (n, nb * 32)).astype(np.uint8)
+    scale = rng.integers(112, 123, (n, nb)).astype(np.uint8)
+    for row, most, byte in ((1, 3, 254), (n // 2, 5, 253), (2, 7, 254), (n - 1, 7, 253)):
+        for blk in (0, nb // 2, nb - 1):
+            code[row, 32 * blk:32 * blk + 32] = rng.integers(1, most + 1, 32)
+            if most == 7:
+                code[row, 32 * blk] = 7
+            scale[row, blk] = byte
+    code[:, k:] = 0
+    q = zs.MXFP4(torch.from_numpy(ref.pack(code)).cuda(), torch.from_numpy(scale).cuda(), k)
+    return q, ref.values(code, scale, k)
+
+
+@pytest.mark.parametrize("x_name", ("f16", "bf16"))
+@pytest.mark.parametrize("m,n,k", [
+    # few rows, the left operand in registers: blocks that do and do not fill steps of four
+    (1, 40, 256), (3, 333, 288), (16, 200, 1600), (2, 200, 1570), (20, 200, 330), (31, 77, 4096),
+    # read at each step; tiles of 64
+    (3, 50, 70), (40, 100, 333), (90, 150, 288), (200, 300, 1030)])
+def test_scale_bytes_253_and_254(zs, x_name, m, n, k):
+    """Values below 2^128 are exact in every product.  From there on a value is
+    as infinite as fp32 and bfloat16 make it: bfloat16 activations above 0 give
+    +infinity, whatever the number of blocks, fp16 ones something not finite,
+    and no other output is touched.  The product of two 4-bit operands takes
+    the value as it is."""
+    import torch
+    say(f"scale bytes 253, 254 {x_name} {m} {n} {k}")
+    rng = np.random.default_rng(m + n + k)
+    xv, dyv = (rounded((np.abs(rng.standard_normal(s)) + 0.5) * 2.0 ** -12, x_name)
+               for s in ((m, k), (m, n)))
+    w, wv = top_scales(zs, n, k, 7)
+    huge = np.abs(wv) >= 2.0 ** 128
+    fin = np.where(huge, 0.0, wv)
+    y, dx = torch.empty(m, n, device="cuda"), torch.empty(m, k, device="cuda")
+    zs.zero_mxfp4_linear(dev(xv, x_name), w, y)
+    zs.zero_mxfp4_linear_grad_input(dev(dyv, x_name), w, dx)
+    for got, a, bt, hit in ((host(y), xv, fin.T, huge.any(1)), (host(dx), dyv, fin, huge.any(0))):
+        assert hit.any() and not hit.all()
+        assert not np.isfinite(got[:, hit]).any()
+        if x_name == "bf16":
+            assert (got[:, hit] == np.inf).all()
+        check_product(got[:, ~hit], a, bt[:, ~hit], "f32", "beside values past 2^128")
+    xq = zs.MXFP4.empty(m, k)
+    zs.zero_mxfp4_quantize(dev(xv, x_name), xq)
+    code, scale, _ = ref.quantize(xv)
+    zs.zero_mxfp4_matmul(xq, w, y)
+    check_product(host(y), ref.values(code, scale, k), wv.T, "f32", "matmul")

@@ -422,7 +422,8 @@ __device__ __forceinline__ void split_f16(const f16x8 &x, bf16x8 &hi, bf16x8 &lo
 }
 
 // Eight codes (one dword) as bfloat16 values times 2^(byte - 127): two
-// significant bits, exact.
+// significant bits, exact below 2^128 (from there on, which only the bytes 253
+// and 254 reach, infinite).
 __device__ __forceinline__ bf16x8 decode8_bf16(uint32_t code, float s) {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 0);
     const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 1);
@@ -594,9 +595,12 @@ struct LeftRows {
 #pragma unroll 1
             for (uint32_t i = 0; i < 4 * count; i++) {
                 const uint32_t k = k0 + 128u * (i / 4) + 8u * (i % 4);
-                const uint32_t blk = k / 32u < nb ? k / 32u : nb - 1;
-                const uint32_t code = *(const uint32_t *)(codes + blk * 16u + 4u * (i % 4));
-                const bf16x8 wf = decode8_bf16(code, __uint_as_float((uint32_t)scales[blk] << 23));
+                uint32_t code = 0, byte = 127;
+                if (k / 32u < nb) {
+                    code = *(const uint32_t *)(codes + k / 32u * 16u + 4u * (i % 4));
+                    byte = scales[k / 32u];
+                }
+                const bf16x8 wf = decode8_bf16(code, __uint_as_float(byte << 23));
 #pragma unroll
                 for (int t = 0; t < MT; t++) {
                     bf16x8 hi, lo;
@@ -651,8 +655,8 @@ struct LeftMx {
     }
 };
 
-// nb >= 8.  A lane's block past the last one repeats that one against zeros
-// of the left operand (a NaN block makes its outputs NaN anyway).
+// nb >= 8.  A lane's block past the last one repeats that one's codes with a
+// scale of 2^-127, which keeps them finite, against zeros of the left operand.
 template <class Left, int OCC>
 __global__ __launch_bounds__(kSkinnyWaves * 64, OCC) void zs_mx_rows_kernel(
     const typename Left::T *x, uint64_t ld_x, MxArgs a, MxArgs w, uint64_t M, uint64_t N,
@@ -665,6 +669,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64, OCC) void zs_mx_rows_kernel(
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t steps = (nb + 3) / 4, first = skinny_first(steps, wave);
     const uint32_t count = skinny_first(steps, wave + 1) - first;
+    constexpr uint32_t kPast = 0x0C0C0C0Cu; // selects a byte of 0
     uint32_t code_at[S], pair_at[S / 2], sel[S];
 #pragma unroll
     for (uint32_t i = 0; i < S; i++) {
@@ -672,8 +677,8 @@ __global__ __launch_bounds__(kSkinnyWaves * 64, OCC) void zs_mx_rows_kernel(
         code_at[i] = (blk < nb ? blk : nb - 1) * 16u;
         const uint32_t pair = 4u * (first + (i & ~1u)), p = pair + 8u <= nb ? pair : nb - 8u;
         pair_at[i / 2] = p;
-        const uint32_t byte = (blk < nb ? blk : nb - 1) - p;
-        sel[i] = 0x0C0C0C00u | (byte < 7u ? byte : 7u);
+        const uint32_t byte = blk - p;
+        sel[i] = blk < nb ? 0x0C0C0C00u | (byte & 7u) : kPast;
     }
     struct Weight {
         u32x4 c[S];
@@ -747,7 +752,8 @@ __global__ __launch_bounds__(kSkinnyWaves * 64, OCC) void zs_mx_rows_kernel(
                 const uint32_t byte = __builtin_amdgcn_perm((uint32_t)(now.b[i / 2] >> 32),
                                                             (uint32_t)now.b[i / 2], sel[i]);
                 if (Left::kChecks)
-                    fits &= fits_f16(byte, now.c[i][0] | now.c[i][1] | now.c[i][2] | now.c[i][3]);
+                    fits &= sel[i] == kPast ||
+                            fits_f16(byte, now.c[i][0] | now.c[i][1] | now.c[i][2] | now.c[i][3]);
                 left.multiply(acc, i, now.c[i], byte);
             }
         if (Left::kChecks && !fits)
