@@ -11,7 +11,7 @@ import pytest
 from test_mx_distill_host import B, EHIP, EINVAL, EOVERFLOW, F16, F32, ROOT, mx
 
 
-@pytest.mark.parametrize("body", ["empty_workspace", "many_rows"])
+@pytest.mark.parametrize("body", ["empty_workspace", "many_rows", "gradient_parts"])
 def test_limits(body):
     env = dict(os.environ, HIP_VISIBLE_DEVICES="", CUDA_VISIBLE_DEVICES="",
                ROCR_VISIBLE_DEVICES="")
@@ -56,3 +56,25 @@ def many_rows(zs):
     w = mx(zs, (1 << 30) + 1, 32, scales=B + (1 << 39))
     assert L.zero_mxfp4_linear(5 * B, F16, 1, 32, ctypes.byref(w), 7 * B, F32, 1 << 31,
                                None) == EOVERFLOW
+
+
+def gradient_parts(zs):
+    """The workspace is 0 where the whole sum is faster: 256 x 256 tiles that
+    fill a round, and sums too short for their parts."""
+    L = zs.lib()
+    for m, n, k, parts in (
+            # 256 x 256 tiles: one round, two thirds of one, more than one
+            (4096, 4096, 4096, 1), (4096, 11_008, 4096, 1), (4096, 32_000, 4096, 1),
+            (8192, 6400, 1600, 1), (8192, 32_000, 1600, 1), (4352, 4096, 2048, 1),
+            (4352, 9216, 2048, 3), (4352, 11_008, 2048, 3), (8704, 32_000, 1280, 3),
+            (8960, 32_000, 1280, 1), (8192, 50_257, 4096, 1),
+            # 128 x 128, one a CU
+            (2048, 4096, 2048, 1), (2048, 6144, 2048, 2), (2048, 32_000, 2048, 2),
+            (2304, 11_008, 2304, 1),
+            # 64 x 64, many and few
+            (1024, 2048, 1024, 1), (512, 2048, 1600, 1), (512, 4096, 1600, 2),
+            (65, 2048, 4096, 2), (65, 50_257, 1600, 10), (512, 4096, 4096, 1)):
+        n_bytes = ctypes.c_uint64(7)
+        assert L.zero_mxfp4_grad_workspace(m, ctypes.byref(mx(zs, n, k)),
+                                           ctypes.byref(n_bytes)) == 0
+        assert n_bytes.value == (parts * m * k * 4 if parts > 1 else 0), (m, n, k)

@@ -2011,24 +2011,43 @@ extern "C" int zero_mxfp4_linear(const void *x, int x_type, uint64_t m, uint64_t
                               : linear<BF16>(x, m, ld_x, w, y, y_type, ld_y, st);
 }
 
-// Parts of the sum over the weight's rows: the kernel for few rows gets a
+// Parts of the sum over the weight's rows.  The kernel for few rows gets a
 // workgroup for each CU, each wave a unit of 32 rows at least (two a CU read
-// more of dy and join more: 64 x 50257 x 1600 77 us against 68, four 90); the
-// tiled one, whose 64 x 64 tiles run two a CU, two, of 16 units of 64 rows at
-// least (65 rows of the same 78 us, with one a CU 120; 512 x 4096 x 4096 stays
-// whole at 53, in four parts 66).  Whole sums took 525 and 548 us, 1 x 50257 x
-// 1600 153 (30 now).  The join takes a grid of at most 65,535 rows.
+// more of dy and join more: 64 x 50257 x 1600 77 us against 68, four 90); whole
+// sums took 525 us there, 153 for 1 x 50257 x 1600 (30 now).
+// The tiled kernels run two workgroups a CU, of 256 x 256 tiles one.  A part is
+// worth its partial sums and the join where it holds enough steps of 64 rows
+// (m x n x k, bfloat16, whole against in parts):
+// - 64 x 64: 16 for up to 128 tiles (65 x 50257 x 1600 548 us against 78; 65 x
+//   2048 x 4096 20 and 17), 32 for more (512 x 2048 x 1600 20.8 against 25.4 in
+//   two parts, 512 x 4096 x 1600 47 and 36);
+// - 128 x 128: 48 (2048 x 4096 x 2048 54 and 60, 2048 x 6144 x 2048 80 and 80,
+//   2048 x 32000 x 2048 381 and 328);
+// - 256 x 256: three parts of up to 170 tiles take two thirds of a round: 48
+//   (4352 x 4096 x 2048 122 and 129, 4352 x 11008 x 2048 298 and 250).  Two parts
+//   are two half rounds, as long as one, and cost 50-60 us more (4096 x 4096 x
+//   4096 123 and 175): only the fp32 sums of 768 steps and more are halved, for
+//   3-4% (4096 x 50257 x 4096 1661 and 1726).
+// The join takes a grid of at most 65,535 rows.
 static uint32_t grad_parts(uint64_t m, uint64_t N, uint64_t K) {
+    if (m > 65535)
+        return 1;
     uint64_t want, most;
     if (m <= kSkinnyM) {
         want = kCUs / ((K + kGradCols - 1) / kGradCols);
         most = (N + 31) / 32 / (m <= 16 ? grad_waves(1) : grad_waves(4));
     } else {
-        want = 2 * kCUs / tiles_of(m, K, 32 * tile_frags(m, K, kCUs));
-        most = (N + 63) / 64 / 16;
+        const int frags = tile_frags(m, K, kCUs);
+        const uint64_t tiles = tiles_of(m, K, 32 * frags), steps = (N + 63) / 64;
+        want = 2 * kCUs / tiles;
+        most = steps / (frags == 2 ? (tiles > kCUs / 2 ? 32 : 16)
+                        : frags == 4 || want == 3 ? 48
+                                                  : 384);
+        if (frags == 8 && most < want) // all of them or none
+            most = 1;
     }
     const uint64_t parts = want < most ? want : most;
-    return parts < 2 || m > 65535 ? 1 : (uint32_t)parts;
+    return parts < 2 ? 1 : (uint32_t)parts;
 }
 
 template <class Fmt>
