@@ -22,7 +22,8 @@ SOURCES = [os.path.join(HERE, "csrc", f)
                      "zs_distill.hip")]
 HEADERS = [os.path.join(ROOT, "include", "zero_shard.h"),
            os.path.join(HERE, "csrc", "zs_internal.h"),
-           os.path.join(HERE, "csrc", "zs_ops.h")]
+           os.path.join(HERE, "csrc", "zs_ops.h"),
+           os.path.join(HERE, "csrc", "zs_mx_rules.h")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

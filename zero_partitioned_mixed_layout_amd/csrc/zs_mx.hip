@@ -14,9 +14,12 @@
 
 #include "zero_shard.h"
 #include "zs_internal.h"
+#include "zs_mx_rules.h"
 #include "zs_ops.h"
 
 namespace {
+
+using namespace zs::mx;
 
 using zs::f32x4;
 using zs::u32x4;
@@ -320,9 +323,6 @@ struct Const {
 // past its registers, less than eight blocks.  Bound by the loads of the left
 // operand: 64 x 4096 x 4096 in bfloat16 19 us.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kSkinnyWaves = 8;
-constexpr uint64_t kSkinnyM = 64;
-
 struct MxArgs {
     const uint8_t *codes;
     const uint8_t *scales;
@@ -1437,9 +1437,6 @@ __global__ __launch_bounds__(kTileThreads, FM == 8 ? 2 : 4) void zs_mx_half_tile
 // (l % 16) + e, so that lane l of the result holds the columns 16 (l / 16) +
 // 4 i + e of row l % 16 and no shared memory is needed before the join.
 // ---------------------------------------------------------------------------
-constexpr uint32_t grad_waves(int mt) { return mt == 1 ? 16 : 8; }
-constexpr uint32_t kGradCols = 64;
-
 template <class Fmt, int MT>
 struct GradSkinnyData {
     uint32_t code[8], byte[8];
@@ -1818,35 +1815,6 @@ static dim3 skinny_grid(uint64_t N) {
                : dim3((uint32_t)kSkinnyGridX, (uint32_t)((groups + kSkinnyGridX - 1) / kSkinnyGridX));
 }
 
-// Tiles of a tiled product: 256 x 256 if they take more than half of the
-// chip's 256 CUs (one of them a CU), else 128 x 128 if there are `least` of
-// those (two a CU), else 64 x 64.  Measured at K = 4096, N = 4096, bfloat16
-// linear: 2048 rows (128 tiles of 256, 512 of 128) 103 us against 87; 2047 x
-// 6400 x 1600 (200 and 800) 49 against 65; 512 rows (128 of 128, 512 of 64)
-// 69 against 43.  In 4 bits a step has half the loads and no decoding, and
-// 128 x 128 pays earlier: 512 rows 18 us against 25.
-constexpr uint64_t kCUs = 256;
-static uint64_t tiles_of(uint64_t M, uint64_t C, uint64_t tile) {
-    return (M + tile - 1) / tile * ((C + tile - 1) / tile);
-}
-static int tile_frags(uint64_t M, uint64_t C, uint64_t least) {
-    return tiles_of(M, C, 256) > kCUs / 2 ? 8 : tiles_of(M, C, 128) >= least ? 4 : 2;
-}
-
-// Whether the skinny kernels take a product: 17 and more rows make each of
-// their workgroups read much of the left operand, and from 33 rows on 64 x 64
-// tiles are faster if they fill half the chip (64 rows, K = 4096: N = 4096 19
-// us against 28 tiled, N = 11008 51 against 29).
-static bool skinny(uint64_t M, uint64_t N) {
-    return M <= kSkinnyM / 2 || (M <= kSkinnyM && tiles_of(M, N, 64) < kCUs / 2);
-}
-
-// Whether the kernel that holds the left operand in registers takes a
-// product: `most` steps a wave hold K.
-static bool in_registers(uint64_t nb, uint32_t most) {
-    return nb >= 8 && nb <= 4ull * kSkinnyWaves * most;
-}
-
 // Workgroups: as many as the registers let run at once, taking the groups in
 // turn (dealt evenly over fewer workgroups, the CUs were not: 5 x 50257 x 1600
 // 12.7 us against 11.9).
@@ -1896,7 +1864,7 @@ extern "C" int zero_mxfp4_matmul(const zero_mxfp4 *a, const zero_mxfp4 *w, void 
     if (K == 0)
         return zero_rows(y, y_type, M, N, ld_y, st);
     if (!skinny(M, N)) {
-        switch (tile_frags(M, N, kCUs / 4)) {
+        switch (tile_frags(M, N, kLeastTilesMx)) {
         case 8:
             return launch_matmul_tiles<8, 4>(a, w, y, y_type, ld_y, st);
         case 4:
@@ -1947,7 +1915,7 @@ template <class Fmt, template <class, uint32_t> class Stage>
 static int half_tiles(const void *x, uint64_t ld_x, const zero_mxfp4 *w, uint64_t M, uint64_t C,
                       uint64_t I, void *y, int y_type, uint64_t ld_y, const Part &split,
                       hipStream_t st) {
-    switch (tile_frags(M, C, kCUs)) {
+    switch (tile_frags(M, C, kLeastTilesHalf)) {
     case 8:
         return launch_half_tiles<Fmt, Stage, 8, 4, 1>(x, ld_x, w, M, C, I, y, y_type, ld_y, split,
                                                        st);
@@ -2009,45 +1977,6 @@ extern "C" int zero_mxfp4_linear(const void *x, int x_type, uint64_t m, uint64_t
         return zero_rows(y, y_type, m, w->rows, ld_y, st);
     return x_type == ZERO_F16 ? linear<F16>(x, m, ld_x, w, y, y_type, ld_y, st)
                               : linear<BF16>(x, m, ld_x, w, y, y_type, ld_y, st);
-}
-
-// Parts of the sum over the weight's rows.  The kernel for few rows gets a
-// workgroup for each CU, each wave a unit of 32 rows at least (two a CU read
-// more of dy and join more: 64 x 50257 x 1600 77 us against 68, four 90); whole
-// sums took 525 us there, 153 for 1 x 50257 x 1600 (30 now).
-// The tiled kernels run two workgroups a CU, of 256 x 256 tiles one.  A part is
-// worth its partial sums and the join where it holds enough steps of 64 rows
-// (m x n x k, bfloat16, whole against in parts):
-// - 64 x 64: 16 for up to 128 tiles (65 x 50257 x 1600 548 us against 78; 65 x
-//   2048 x 4096 20 and 17), 32 for more (512 x 2048 x 1600 20.8 against 25.4 in
-//   two parts, 512 x 4096 x 1600 47 and 36);
-// - 128 x 128: 48 (2048 x 4096 x 2048 54 and 60, 2048 x 6144 x 2048 80 and 80,
-//   2048 x 32000 x 2048 381 and 328);
-// - 256 x 256: three parts of up to 170 tiles take two thirds of a round: 48
-//   (4352 x 4096 x 2048 122 and 129, 4352 x 11008 x 2048 298 and 250).  Two parts
-//   are two half rounds, as long as one, and cost 50-60 us more (4096 x 4096 x
-//   4096 123 and 175): only the fp32 sums of 768 steps and more are halved, for
-//   3-4% (4096 x 50257 x 4096 1661 and 1726).
-// The join takes a grid of at most 65,535 rows.
-static uint32_t grad_parts(uint64_t m, uint64_t N, uint64_t K) {
-    if (m > 65535)
-        return 1;
-    uint64_t want, most;
-    if (m <= kSkinnyM) {
-        want = kCUs / ((K + kGradCols - 1) / kGradCols);
-        most = (N + 31) / 32 / (m <= 16 ? grad_waves(1) : grad_waves(4));
-    } else {
-        const int frags = tile_frags(m, K, kCUs);
-        const uint64_t tiles = tiles_of(m, K, 32 * frags), steps = (N + 63) / 64;
-        want = 2 * kCUs / tiles;
-        most = steps / (frags == 2 ? (tiles > kCUs / 2 ? 32 : 16)
-                        : frags == 4 || want == 3 ? 48
-                                                  : 384);
-        if (frags == 8 && most < want) // all of them or none
-            most = 1;
-    }
-    const uint64_t parts = want < most ? want : most;
-    return parts < 2 ? 1 : (uint32_t)parts;
 }
 
 template <class Fmt>
