@@ -100,3 +100,28 @@ def test_scale_bytes_253_and_254(zs, x_name, m, n, k):
     code, scale, _ = ref.quantize(xv)
     zs.zero_mxfp4_matmul(xq, w, y)
     check_product(host(y), ref.values(code, scale, k), wv.T, "f32", "matmul")
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1000, 4096), (5, 257, 31), (33, 1600, 160), (65, 129, 257),
+                                   (130, 70, 2048), (1030, 1029, 300)])
+def test_matmul_rounds_to_fp16_infinity(zs, m, n, k):
+    """Operands whose sums pass fp16's range: a sum from 65520 on, where fp16
+    rounds to infinity, is infinite with its sign; below it is the sum rounded
+    once; within the sum's own error of 65520 the computed sum, which lies
+    within that error of the exact one, may be on either side."""
+    import torch
+    say(f"matmul fp16 overflow {m} {n} {k}")
+    a, av = random_mx(zs, m, k, 1)
+    w, wv = random_mx(zs, n, k, 2, pad_codes=16 * (k % 3), pad_scales=k % 5)
+    y = torch.zeros(m, n, dtype=torch.float16, device="cuda")
+    zs.zero_mxfp4_matmul(a, w, y)
+    got, want = host(y), av @ wv.T
+    tol = (k + 8) * 2.0 ** -23 * (np.abs(av) @ np.abs(wv).T)
+    over, under = np.abs(want) - tol >= 65520.0, np.abs(want) + tol < 65520.0
+    assert under.any() and (over.any() or k == 31) and np.mean(over | under) > 0.98
+    assert np.array_equal(got[over], np.copysign(np.inf, want[over]))
+    half = ref.HALF_STEP["f16"] * (np.abs(want) + tol) + tol + ref.SMALLEST["f16"]
+    fits = np.abs(got - want) <= half
+    assert fits[under].all()
+    near = ~over & ~under
+    assert (fits | (got == np.copysign(np.inf, want)))[near].all()
