@@ -623,6 +623,11 @@ int zero_adam_step_noalloc(const zero_tensor *tensors, uint32_t n_tensors,
  * (zero_mxfp4_quantize writes them so).  A flat shard is a matrix of one
  * row; where cols is a multiple of 32 and the pitches are the dense ones,
  * the matrix and the flat array of rows * cols values have the same bytes.
+ *
+ * The entry points from here on refuse arrays that overlap where one of them
+ * is written.  An array with a row pitch counts as the span from its first
+ * byte to its last: two whose rows lie between each other's, as columns of one
+ * buffer do, are refused although they share no byte.
  */
 typedef struct zero_mxfp4 {
     void *codes;        /* device; row r at r * ld_codes; 16-byte aligned */
@@ -655,7 +660,8 @@ int zero_mxfp4_layout(uint64_t rows, uint64_t cols, zero_mxfp4 *out);
  *   is infinite or NaN.
  * Asynchronous; allocates nothing; no rows or no columns: launches nothing.
  * Errors: EINVAL (NULL, a bad type, pitch or alignment, overlapping
- * arrays); EOVERFLOW; EHIP.
+ * arrays); EOVERFLOW (more than 2^31 - 128 blocks in all, an array past the
+ * address space); EHIP.
  */
 int zero_mxfp4_quantize(const void *src, int src_type, uint64_t ld_src, const zero_mxfp4 *dst,
                         int32_t *nonfinite_flag, void *stream);
@@ -694,8 +700,11 @@ int zero_gather_shards_mxfp4(const void *const *codes, const void *const *scales
  * Products with a 4-bit weight w of N rows and K columns (w->rows, w->cols),
  * read as it is.  Sums are kept in fp32 and rounded once to the output's
  * type (ZERO_F16, ZERO_BF16 or ZERO_F32).  The order of a sum depends on the
- * sizes alone, so equal calls give equal bits.  Infinities and NaN follow
- * IEEE: a NaN block of w (scale byte 255) makes every output it enters NaN.
+ * sizes and, for fp16 x or dy, on where w has blocks outside fp16's range (a
+ * NaN block, or a nonzero one with a scale byte outside 104 to 140: the sums
+ * near it are taken again, exactly but many times slower); equal calls give
+ * equal bits.
+ * Infinities and NaN follow IEEE: a NaN block of w (scale byte 255) makes every output it enters NaN.
  * A value of 2^128 or more, which only the scale bytes 253 and 254 reach and
  * zero_mxfp4_quantize never writes, is past fp32: with a 16-bit operand it is
  * an infinity and makes every output it enters infinite or NaN.
@@ -718,7 +727,7 @@ int zero_gather_shards_mxfp4(const void *const *codes, const void *const *scales
  *   borrowed until the call's work is done), in which a sum over many rows n
  *   for few dx is taken in parts and joined in order.  Less than
  *   zero_mxfp4_grad_workspace names means fewer parts (the order of a sum
- *   depends on the sizes and the number of parts).  Calls that may overlap
+ *   depends on the number of parts too).  Calls that may overlap
  *   must not share one.
  * x, dy: m rows of x_type / dy_type (ZERO_F16 or ZERO_BF16) with a row pitch
  * in elements, any element alignment.

@@ -569,6 +569,8 @@ __global__ __launch_bounds__(NT, NV <= 8 ? 8 : 4) void zs_distill_kernel(Distill
 // kMinSplit elements of the row to write (every one of them reads the whole
 // row for its statistics, from cache, which needs no second launch and no
 // memory between the two).  60 rows of 131,072: 21 us, with 512 workgroups 38.
+// In place a row stays with one workgroup, which has read all of it before it
+// writes: 5 x 50257 fp16 12.5 us against 10.5 apart, 60 x 131072 21.1 and 19.4.
 constexpr uint64_t kFullRows = 256;
 constexpr uint64_t kMinSplit = 4096;
 
