@@ -703,8 +703,8 @@ int zero_gather_shards_mxfp4(const void *const *codes, const void *const *scales
  * sizes and, for fp16 x or dy, on where w has blocks outside fp16's range (a
  * NaN block, or a nonzero one with a scale byte outside 104 to 140: the sums
  * near it are taken again, exactly but many times slower); equal calls give
- * equal bits.
- * Infinities and NaN follow IEEE: a NaN block of w (scale byte 255) makes every output it enters NaN.
+ * equal bits.  Infinities and NaN follow IEEE: a NaN block of w (scale byte
+ * 255) makes every output it enters NaN.
  * A value of 2^128 or more, which only the scale bytes 253 and 254 reach and
  * zero_mxfp4_quantize never writes, is past fp32: with a 16-bit operand it is
  * an infinity and makes every output it enters infinite or NaN.
@@ -727,8 +727,8 @@ int zero_gather_shards_mxfp4(const void *const *codes, const void *const *scales
  *   borrowed until the call's work is done), in which a sum over many rows n
  *   for few dx is taken in parts and joined in order.  Less than
  *   zero_mxfp4_grad_workspace names means fewer parts (the order of a sum
- *   depends on the number of parts too).  Calls that may overlap
- *   must not share one.
+ *   depends on the number of parts too).  Calls that may overlap must not
+ *   share one.
  * x, dy: m rows of x_type / dy_type (ZERO_F16 or ZERO_BF16) with a row pitch
  * in elements, any element alignment.
  */
